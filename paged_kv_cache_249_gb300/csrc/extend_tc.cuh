@@ -207,7 +207,7 @@ __device__ __noinline__ void tc_redo_rows(const ExtArgs &a, ExtTile t, int kvh, 
 struct TcForm {
     float scale;            // of a score
     float cap, in_e;        // softcap; x = scale q.k / cap: 2 x / q.k in log2 units
-    float small;            // |q.k| up to which |x| <= 0.3
+    float small;            // |q.k| up to which |x| <= 0.3: the polynomial's range
     float c1, c3, c5, c7;   // cap tanh(x) = v (c1 + c3 v^2 + c5 v^4 + c7 v^6) with v = q.k, |x| <= 0.3
     bool capped, biased, both_ways;
 };
@@ -219,7 +219,8 @@ __device__ __forceinline__ TcForm tc_form(const ExtArgs &a) {
     f.cap = a.softcap * kTcLog2e;
     const float in = f.capped ? fabsf(a.scale) / a.softcap : 0.f;
     f.in_e = 2.f * kTcLog2e * in;
-    f.small = in <= 1e4f ? 0.3f / in : -1.f;  // (beyond, the coefficients may overflow)
+    // (of larger `in` the coefficients may overflow, of larger q.k their square)
+    f.small = in <= 1e4f ? fminf(0.3f / in, 1e19f) : -1.f;
     // tanh(x) / x as a polynomial in x^2, fitted on |x| <= 0.3: off by 4.3e-8 at most
     const float q = in * in;
     f.c1 = f.scale, f.c3 = -0.333332865f * f.scale * q, f.c5 = 0.133239105f * f.scale * q * q,
@@ -227,10 +228,17 @@ __device__ __forceinline__ TcForm tc_form(const ExtArgs &a) {
     return f;
 }
 
-// W scores q.k (of a row, for adjacent keys) capped and biased, in log2 units.
+// W scores q.k (of a row, for adjacent keys) capped and biased, in log2 units;
+// they are in s, and in TMEM from column `col` on, where they may be overwritten.
 // `dist`: the row's position less the first key's.
+//
+// A score's cap is a function of that score alone: the polynomial up to `small`,
+// above it cap (1 - 2 / (1 + e^(2 x))), whose error of some 2^-22 of the cap a
+// small score would not bear.  Other scores of the warp, among them those of
+// keys that a row does not see, decide only whether the second form is computed
+// at all.
 template <int W>
-__device__ __forceinline__ void tc_modify(float *s, const TcForm &f, float slope, int dist) {
+__device__ __forceinline__ void tc_modify(float *s, uint32_t col, const TcForm &f, float slope, int dist) {
     if (f.capped) {
         float big = 0.f, also = 0.f;
 #pragma unroll
@@ -241,7 +249,7 @@ __device__ __forceinline__ void tc_modify(float *s, const TcForm &f, float slope
         big = fmaxf(big, also);
         if (__all_sync(0xffffffffu, big <= f.small)) {
             // the FMA pipe has room where the exponential and the reciprocal of
-            // the exact form would fill theirs
+            // the other form would fill theirs
             const F2 c1 = f2_pack(f.c1, f.c1), c3 = f2_pack(f.c3, f.c3), c5 = f2_pack(f.c5, f.c5),
                      c7 = f2_pack(f.c7, f.c7);
 #pragma unroll
@@ -250,10 +258,30 @@ __device__ __forceinline__ void tc_modify(float *s, const TcForm &f, float slope
                 f2_unpack(f2_mul(v, f2_fma(t, f2_fma(t, f2_fma(t, c7, c5), c3), c1)), s[e], s[e + 1]);
             }
         } else {
-            // cap tanh(x) = cap (1 - 2 / (1 + e^(2 x)))
+            // The polynomial by single operations, which round alike, in a loop over
+            // the scores in TMEM.  Laid out W times, this code made the other branch
+            // slower (mixed step 179.7 -> 184.2 us) and took longer itself (8 chunks
+            // of 700 tokens over 2300, head_dim 128, cap 5: 396 -> 440), as packed
+            // operations did, whose constants stay in registers (183.9, 414).
+#pragma unroll 1
+            for (int n = 0; n < W; n += 16) {
+                float u[16];
+                tmem_ld16_now(col + n, u);
 #pragma unroll
-            for (int e = 0; e < W; ++e)
-                s[e] = fmaf(-2.f * f.cap, fast_rcp(1.f + fast_exp2(s[e] * f.in_e)), f.cap);
+                for (int e = 0; e < 16; ++e) {
+                    const float v = u[e], t = v * v;
+                    const float near = v * fmaf(t, fmaf(t, fmaf(t, f.c7, f.c5), f.c3), f.c1);
+                    const float far = fmaf(-2.f * f.cap, fast_rcp(1.f + fast_exp2(v * f.in_e)), f.cap);
+                    u[e] = fabsf(v) <= f.small ? near : far;
+                }
+                tmem_st16(col + n, u);
+            }
+            tmem_wait_st();
+#pragma unroll
+            for (int n = 0; n < W; n += 32) tmem_ld32(col + n, s + n);
+            tmem_wait_ld();
+#pragma unroll
+            for (int n = 0; n < W; n += 32) tmem_pin32(s + n);
         }
     }
     if (f.biased) {
@@ -389,13 +417,15 @@ __global__ void __launch_bounds__(TcShape<D, NQ>::kThreads, TcShape<D, NQ>::kCta
     const uint32_t tmem = __shfl_sync(0xffffffffu, c.tmem, 0);
 
     if (warp < kLoadWarp) {
-        // queries, in the 128-byte swizzle the products read; what the rows behind
-        // the last hold reaches no other row
+        // queries, in the 128-byte swizzle the products read; the softmax warps'
+        // rows behind the last are zero, so that no time or result depends on what
+        // the memory held
         constexpr int C = D / 8, kStep = kLoadWarp * 32 / C;
         const int ch = tid % C, step_tok = kStep / G, step_g = kStep % G;
         int tok = (t.row0 + tid / C) / G, g = t.row0 + tid / C - tok * G;
+        int r = tid / C;
 #pragma unroll 2
-        for (int r = tid / C; r < t.nrows; r += kStep) {
+        for (; r < t.nrows; r += kStep) {
             const uint32_t dst = smem_u32(qs) + (r / 128) * S::kQBytes + swz_offset<128>(r % 128, ch);
             const void *src = static_cast<const T *>(a.q) +
                               ((size_t)(t.q0 + tok) * a.num_heads + kvh * G + g) * D + ch * 8;
@@ -403,9 +433,10 @@ __global__ void __launch_bounds__(TcShape<D, NQ>::kThreads, TcShape<D, NQ>::kCta
             tok += step_tok, g += step_g;
             if (g >= G) g -= G, ++tok;
         }
+        for (; r < active * 32; r += kStep) sts_zero16(smem_u32(qs) + (r / 128) * S::kQBytes + swz_offset<128>(r % 128, ch));
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (a.scale < 0.f) {  // the products take |scale|
-            for (int r = tid / C; r < t.nrows; r += kStep) {
+            for (r = tid / C; r < t.nrows; r += kStep) {
                 uint4 *p = reinterpret_cast<uint4 *>(qs + (r / 128) * S::kQBytes + swz_offset<128>(r % 128, ch));
                 uint4 v = *p;
                 v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
@@ -633,7 +664,7 @@ __global__ void __launch_bounds__(TcShape<D, NQ>::kThreads, TcShape<D, NQ>::kCta
                     tmem_ld32(scol + n, s), tmem_ld32(scol + n + 32, s + 32);
                     tmem_wait_ld();
                     tmem_pin32(s), tmem_pin32(s + 32);
-                    if constexpr (MODS) tc_modify<64>(s, form, slope, pos - k);
+                    if constexpr (MODS) tc_modify<64>(s, scol + n, form, slope, pos - k);
                     if (masked()) {
 #pragma unroll
                         for (int i = 0; i < 64; i += 32) {
