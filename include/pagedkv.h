@@ -438,12 +438,13 @@ pkv_status pkv_paged_attention_decode_shared_prefix_run(
  *   larger ones.  Two calls that can overlap on the GPU need one each.
  *
  * Faults, as bits of the pool's error word: a sequence whose query_starts
- *   entries are out of order, out of range, or further apart than
- *   max_query_len sets PKV_FAULT_QUERY and is not computed (nor, perhaps,
- *   its neighbours); one with more new tokens than its context (of at least
- *   one) sets PKV_FAULT_QUERY and gets zeros; context lengths and block
- *   numbers fault as in the decode, and an unusable block's keys are seen by
- *   no token.
+ *   entries are further apart than max_query_len sets PKV_FAULT_QUERY and is
+ *   not computed; the others are.  Entries out of order or out of range set it
+ *   too: then any row may stay as it was (a split call's all do, as a rule), and
+ *   rows that two sequences claim are not specified.  A sequence with more new
+ *   tokens than its context (of at least one) sets PKV_FAULT_QUERY and gets
+ *   zeros; context lengths and block numbers fault as in the decode, and an
+ *   unusable block's keys are seen by no token.
  * A key or value that is not finite reaches only the tokens that see it.
  * Scores, maxima, sums and outputs are fp32 until the store.
  * Supported: BF16 and F16 pools of every head size, F32 pools of head_dim 64

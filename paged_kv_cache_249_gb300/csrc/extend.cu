@@ -77,15 +77,25 @@ size_t partial_bytes(long long rows, int head_dim, int parts, size_t *o_bytes) {
 // and log2-sum-exps e_p (-inf: the part saw no key, o_p is not written):
 //   out = sum_p 2^(e_p - M) o_p / sum_p 2^(e_p - M),  M = max_p e_p.
 // One warp per row of a tile; the tiles are those of the attention kernel, so
-// rows that it skipped stay as they were.
+// rows that it skipped stay as they were.  Where query_starts are out of order or
+// out of range, the attention's list of items may have no room for tiles that the
+// search here finds (it has for those of the other wrong descriptions): their
+// parts hold whatever the workspace held, so nothing is joined.
 template <int D>
 __global__ void __launch_bounds__(128) extend_combine_kernel(const ExtArgs a, int rows) {
     constexpr int PER = D / 32;
     griddep_launch();
     griddep_wait();
     const int kvh = blockIdx.x % a.num_kv_heads;
+    bool wrong = false;
+    if (a.num_seqs <= kExtScan)  // (with more, both find tiles by the same search)
+        for (int s = threadIdx.x; s < a.num_seqs; s += 128) {
+            const int q0 = __ldg(a.query_starts + s), q1 = __ldg(a.query_starts + s + 1);
+            wrong |= q0 < 0 || q1 < q0 || q1 > a.num_tokens;
+        }
     ExtTile t;
-    if (!ext_find_tile(a, blockIdx.x / a.num_kv_heads, rows, t)) return;
+    const bool found = ext_find_tile(a, blockIdx.x / a.num_kv_heads, rows, t);
+    if (__syncthreads_or(wrong) || !found) return;
     const int lane = threadIdx.x & 31;
     const int P = max(1, ext_num_parts(a, t));
     for (int r = blockIdx.y * 4 + threadIdx.x / 32; r < t.nrows; r += gridDim.y * 4) {
