@@ -446,7 +446,11 @@ pkv_status pkv_paged_attention_decode_shared_prefix_run(
  *   zeros; context lengths and block numbers fault as in the decode, and an
  *   unusable block's keys are seen by no token.
  * A key or value that is not finite reaches only the tokens that see it.
- * Scores, maxima, sums and outputs are fp32 until the store.
+ * Scores, maxima, sums and outputs are fp32 until the store.  The softmax
+ *   weights of 16-bit pools meet the values in the pool's type: rounded once
+ *   where out_dtype has 16 bits (half a step of the pool's type, relative to each
+ *   weight, which the decode does not round; a token that sees one key still
+ *   gets that value bit by bit), as two parts where it is F32.
  * Supported: BF16 and F16 pools of every head size, F32 pools of head_dim 64
  * and 128; num_heads / num_kv_heads in 1..16.
  */

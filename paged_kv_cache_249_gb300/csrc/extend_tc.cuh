@@ -5,8 +5,9 @@
 // query rows sees, with a running reference m and sum l per row,
 //   S = Q K^T,  P = 2^(f(S) - m),  O += P V,  l += sum P,  out = O / l.
 // S and O live in TMEM.  The softmax reads a row of S, writes P over it in the
-// pool's type, and P is the A operand of P V straight from TMEM.  m moves only
-// when a score passes it by 2^8, so O is rarely rescaled.
+// pool's type, and P is the A operand of P V straight from TMEM.  m is set by the
+// row's first scores and moves only when a later one passes it by 2^8, so O is
+// rarely rescaled.
 //
 // Roles in a CTA: one warp stages K and V (TMA, 16-row runs of the pages, a
 // ring of tiles), one thread per row tile issues the products, four warps per
@@ -38,7 +39,16 @@
 namespace pkv {
 
 constexpr float kTcLog2e = 1.4426950408889634f;
-constexpr float kTcLag = 8.f;  // a row's reference may trail its maximum by 2^8
+// A row's reference is its first maximum, so that a row that sees one key has
+// the weight 1 and gets that value bit by bit; it moves once a score passes it by
+// 2^8.  In fp16, whose small weights have fewer bits, it lies 2^7 lower, which is
+// exact as well: largest weights are 2^7 to 2^15, and bits go from 2^-21 of the
+// largest on, not from 2^-14.
+template <bool BF16>
+struct TcRef {
+    static constexpr float kBelow = BF16 ? 0.f : 7.f;
+    static constexpr float kLag = BF16 ? 8.f : 15.f;
+};
 
 // NQ tiles of 128 rows share each staged tile of K and V.  One: two CTAs per
 // SM, whose loads, products and softmax overlap each other (D = 256 has room
@@ -627,9 +637,8 @@ __global__ void __launch_bounds__(TcShape<D, NQ>::kThreads, TcShape<D, NQ>::kCta
         const TcForm form = tc_form(a);
         // scores in log2 units; a scale of zero stays above it, so that -inf * factor is -inf
         const float factor = MODS ? 1.f : fmaxf(fabsf(a.scale) * kTcLog2e, 1e-30f);
-        // The reference m starts at zero, which serves as long as the row's first
-        // maximum is not far from it.  l is zero until the row has seen a key.
-        constexpr float kTcLow = kBf16 ? -8.f : 0.f;  // fp16 weights have few small values
+        // l is zero until the row has seen a key.
+        using Ref = TcRef<kBf16>;
         float m = 0.f, l = 0.f;
         bool ok = true;
         for (int j = 0; j < ntiles; ++j) {
@@ -691,7 +700,7 @@ __global__ void __launch_bounds__(TcShape<D, NQ>::kThreads, TcShape<D, NQ>::kCta
                 scan([] { return true; });
             }
             const float top = fmaxf(t0, t1) * factor;
-            const bool move = top > m + kTcLag || (l == 0.f && top < m + kTcLow && top > -CUDART_INF_F);
+            const bool move = l == 0.f ? top > -CUDART_INF_F : top > m + Ref::kLag;
             if (__any_sync(0xffffffffu, move)) {
                 const bool scale_o = move && l != 0.f;
                 if (__any_sync(0xffffffffu, scale_o)) {
@@ -699,7 +708,7 @@ __global__ void __launch_bounds__(TcShape<D, NQ>::kThreads, TcShape<D, NQ>::kCta
                     ok = __all_sync(0xffffffffu, tc_wait(c, &c.o_full[q], (j - 1) & 1, a.dev_error));
                     if (!ok) break;
                     tc_fence_after();
-                    const float f = scale_o ? fast_exp2(m - top) : 1.f;
+                    const float f = scale_o ? fast_exp2(m - (top - Ref::kBelow)) : 1.f;
                     l *= f;
 #pragma unroll 1
                     for (int i = 0; i < D / 16; ++i) {
@@ -710,7 +719,7 @@ __global__ void __launch_bounds__(TcShape<D, NQ>::kThreads, TcShape<D, NQ>::kCta
                         tmem_st16(ocol + i * 16, o);
                     }
                 }
-                if (move) m = top;
+                if (move) m = top - Ref::kBelow;
             }
             const F2 f2 = f2_pack(factor, factor), h2 = f2_pack(-m, -m);
             F2 sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
