@@ -153,15 +153,76 @@ __device__ __forceinline__ void tc_clear_values(unsigned char *tile, int lo, int
     fence_proxy_async_smem();
 }
 
-// Rows first + i of a tile, for the bits i of `rows`, again, one at a time on
-// the CUDA cores, straight from the pool, by the warp that has written them:
-// those with a result that is not finite.  It may be right: then it comes out again.  But a
-// value that is not finite at a key that the row does not see, and others of
-// its tile do, reaches it in the product (0 * inf is NaN).
+// Results that are not finite.  The product gives a value at a key that a row does
+// not see, and others of its tile do, the weight zero, and 0 * inf is NaN: a row's
+// NaN may not be its own.  It is where the sum l is NaN (a score that the row sees
+// was).  Where l is a number and a result is not finite, the part's values are looked
+// at, and rows whose result may not be their own are computed again.
+
+// Of one run of keys (16 rows of D values), those with a value that is not finite,
+// and 16 bits further up those with an infinite one.  By a whole warp.
+template <typename T, int D>
+__device__ __forceinline__ uint32_t tc_odd_keys(const T *run) {
+    constexpr uint32_t kInf = __is_same(T, __nv_bfloat16) ? 0x7f80u : 0x7c00u;
+    const int lane = threadIdx.x & 31;
+    uint4 v[D / 16];
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) v[i] = __ldg(reinterpret_cast<const uint4 *>(run) + i * 32 + lane);
+    uint32_t odd = 0;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        bool any = false, inf = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t lo = w[e] & 0x7fffu, hi = (w[e] >> 16) & 0x7fffu;
+            any |= lo >= kInf || hi >= kInf;
+            inf |= lo == kInf || hi == kInf;
+        }
+        odd |= ((any ? 1u : 0u) | (inf ? 0x10000u : 0u)) << ((i * 32 + lane) / (D / 8));
+    }
+    return __reduce_or_sync(0xffffffffu, odd);
+}
+
+// Whether the lane's row has to be computed again (1; 2: with small weights); `nan`: it has a NaN, `inf`: it has
+// an infinity (or nearly) and no NaN.  lo, hi and words: what it sees, as in tc_seen.
+//   - A NaN is the row's own if it sees a NaN, and no value that is not finite lies at
+//     a key that it does not see, nor an infinite one at a key that it does (a weight
+//     that rounds to zero, or has no remainder, makes NaN of it).
+//   - An infinity is its own if it sees one: from another key it would be a NaN.
+//   - Either may come from finite values whose sum passes fp32's range, since the
+//     weights' sum is above 1.  Smaller weights, whose sum is not, keep it within.
+template <typename T, int D>
+__device__ __noinline__ int tc_not_its_own(const ExtArgs &a, const TcControl &c, int seq, int kvh, bool nan,
+                                            bool inf, int lo, int hi, const uint32_t *words) {
+    const int32_t *tbl = a.block_tables + (size_t)seq * a.max_blocks_per_seq;
+    const int first = max(c.k0, c.kmin);  // what lies before was cleared
+    bool sees_nan = false, sees_inf = false, other = false;
+    for (int k = first & ~(kExtRun - 1); k < c.k1; k += kExtRun) {
+        const int run = k / kExtRun, blk = __ldg(tbl + (run >> a.run_shift));
+        if (blk < 0 || blk >= a.num_blocks) continue;
+        const size_t row = ((((size_t)blk * a.num_kv_heads + kvh) << a.run_shift) + (run & ((1 << a.run_shift) - 1))) * kExtRun;
+        const uint32_t odd = tc_odd_keys<T, D>(static_cast<const T *>(a.v_pool) + row * D);
+        if (odd == 0) continue;
+        const uint32_t part = bit_range(first - k, c.k1 - k), see = tc_seen(a, c, lo, hi, words, k, 0, 0);
+        sees_nan |= (odd & part & see & 0xffffu) != 0;
+        sees_inf |= ((odd >> 16) & part & see) != 0;
+        other |= (odd & part & ~see & 0xffffu) != 0;
+        // all is known
+        if (__all_sync(0xffffffffu, nan ? other || sees_inf : !inf || sees_inf)) break;
+    }
+    if (nan ? sees_nan && !sees_inf && !other : !inf || sees_inf) return 0;
+    return sees_nan || sees_inf || other ? 1 : 2;
+}
+
+// Rows first + i of a tile, for the bits i of `rows`, again, one at a time on the
+// CUDA cores, straight from the pool, by the warp that has written them: a key to a
+// lane for the scores, then the columns to the lanes for the values.  Those of
+// `small` with weights 2^-24 times as large.
 template <typename T, int D>
 __device__ __noinline__ void tc_redo_rows(const ExtArgs &a, ExtTile t, int kvh, int k0, int k1,
-                                          int part, int first, uint32_t rows) {
-    constexpr int PER = D / 32;
+                                          int part, int first, uint32_t rows, uint32_t small) {
+    constexpr int PER = D / 32, kVec = 8;
     const int lane = threadIdx.x & 31, G = a.group;
     for (; rows; rows &= rows - 1) {
         const int row = t.row0 + first + __ffs(rows) - 1, tok = row / G, h = kvh * G + row - tok * G;
@@ -170,39 +231,69 @@ __device__ __noinline__ void tc_redo_rows(const ExtArgs &a, ExtTile t, int kvh, 
         int lo = 0, hi = base;
         if (!a.tree_mask) ext_row_range(a, t.prefix, pos, lo, hi);
         const float slope = a.slopes ? __ldg(a.slopes + h) * kTcLog2e : 0.f;
-        float q[PER], o[PER], m = -CUDART_INF_F, l = 0.f;
-        const T *qp = static_cast<const T *>(a.q) + oh * D;
+        const uint4 *qp = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) + oh * D);
+        const float below = (small >> (__ffs(rows) - 1)) & 1u ? 24.f : 0.f;
+        float o[PER], m = -CUDART_INF_F, l = 0.f;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) q[i] = (float)qp[i * 32 + lane], o[i] = 0.f;
-        for (int j = k0; j < k1; ++j) {
-            bool seen = j >= lo && j < hi;
-            if (a.tree_mask && j >= base)
+        for (int i = 0; i < PER; ++i) o[i] = 0.f;
+        const int end = a.tree_mask ? k1 : min(k1, hi);
+        for (int j0 = max(k0, lo) & ~31; j0 < end; j0 += 32) {
+            const int j = j0 + lane;
+            bool seen = j >= k0 && j < k1 && j >= lo && j < hi;
+            if (a.tree_mask && j >= max(base, k0) && j < k1)
                 seen = (__ldg(a.tree_mask + (size_t)(t.q0 + tok) * a.mask_words + ((j - base) >> 5)) >>
                         ((j - base) & 31)) & 1u;
-            if (!seen) continue;
-            const int b = __ldg(a.block_tables + (size_t)t.seq * a.max_blocks_per_seq + j / a.block_size);
-            if (b < 0 || b >= a.num_blocks) continue;
-            const size_t at = (((size_t)b * a.num_kv_heads + kvh) * a.block_size + j % a.block_size) * D;
-            const T *kp = static_cast<const T *>(a.k_pool) + at;
-            const T *vp = static_cast<const T *>(a.v_pool) + at;
-            float x = 0.f;
+            size_t at = 0;
+            if (seen) {
+                const int b = __ldg(a.block_tables + (size_t)t.seq * a.max_blocks_per_seq + j / a.block_size);
+                seen = b >= 0 && b < a.num_blocks;
+                if (seen) at = (((size_t)b * a.num_kv_heads + kvh) * a.block_size + j % a.block_size) * D;
+            }
+            const uint32_t any = __ballot_sync(0xffffffffu, seen);
+            if (any == 0) continue;
+            float x = -CUDART_INF_F;
+            if (seen) {
+                const uint4 *kp = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.k_pool) + at);
+                x = 0.f;
+#pragma unroll 4
+                for (int i = 0; i < D / kVec; ++i) {
+                    const uint4 q = __ldg(qp + i), k = __ldg(kp + i);
+                    const uint32_t qw[4] = {q.x, q.y, q.z, q.w}, kw[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-            for (int i = 0; i < PER; ++i) x = fmaf(q[i], (float)kp[i * 32 + lane], x);
+                    for (int e = 0; e < 4; ++e) {
+                        x = fmaf(Mma16<T>::lo(qw[e]), Mma16<T>::lo(kw[e]), x);
+                        x = fmaf(Mma16<T>::hi(qw[e]), Mma16<T>::hi(kw[e]), x);
+                    }
+                }
+                x *= a.scale;
+                if (a.softcap > 0.f) x = a.softcap * tanhf(x / a.softcap);
+                x = x * kTcLog2e - (a.slopes ? slope * fabsf((float)(pos - j)) : 0.f);
+            }
+            float top = fmaxf(m, x);
 #pragma unroll
-            for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-            x *= a.scale;
-            if (a.softcap > 0.f) x = a.softcap * tanhf(x / a.softcap);
-            x = x * kTcLog2e - (a.slopes ? slope * fabsf((float)(pos - j)) : 0.f);
-            const float top = fmaxf(m, x), ref = top == -CUDART_INF_F ? 0.f : top;
-            const float f = exp2f(m - ref), p = exp2f(x - ref);
+            for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+            const float ref = top == -CUDART_INF_F ? 0.f : top;
+            const float f = exp2f(m - ref), p = seen ? exp2f(x - ref - below) : 0.f;
             m = top;
-            l = l * f + p;
+            l = l * f + p;  // (the lanes' sums are joined at the end)
 #pragma unroll
-            for (int i = 0; i < PER; ++i) o[i] = o[i] * f + p * (float)vp[i * 32 + lane];
+            for (int i = 0; i < PER; ++i) o[i] *= f;
+#pragma unroll 4
+            for (int s = 0; s < 32; ++s) {
+                const float w = __shfl_sync(0xffffffffu, p, s);
+                const size_t from = __shfl_sync(0xffffffffu, at, s);
+                if ((any >> s) & 1u) {
+                    const T *vp = static_cast<const T *>(a.v_pool) + from;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) o[i] = fmaf(w, (float)vp[i * 32 + lane], o[i]);
+                }
+            }
         }
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
         const float inv = l == 0.f ? 0.f : 1.f / l;
         if (a.num_parts > 1 && lane == 0)
-            a.ws_lse[oh * a.num_parts + part] = l == 0.f ? -CUDART_INF_F : m + log2f(l);
+            a.ws_lse[oh * a.num_parts + part] = l == 0.f ? -CUDART_INF_F : m + below + log2f(l);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             if (a.num_parts > 1)
@@ -780,7 +871,7 @@ __global__ void __launch_bounds__(TcShape<D, NQ>::kThreads, TcShape<D, NQ>::kCta
             unsigned char *stage = qs + warp * (32 * 2 * D);  // 32 rows of 2 D bytes
             constexpr int C = 2 * D / 16;                     // chunks of a staged row
             const int nlive = min(32, t.nrows - warp * 32);
-            bool odd = !(fabsf(l) <= 3e38f);
+            bool nan = false, odd = false;
 #pragma unroll 1
             for (int d0 = 0; d0 < D; d0 += type == PKV_F32 ? D / 2 : D) {
                 __syncwarp();
@@ -793,6 +884,7 @@ __global__ void __launch_bounds__(TcShape<D, NQ>::kThreads, TcShape<D, NQ>::kCta
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         v[e] *= inv;
+                        nan |= v[e] != v[e];
                         odd |= !(fabsf(v[e]) <= 3e38f);
                     }
                     uint4 *dst = reinterpret_cast<uint4 *>(stage + lane * (2 * D));
@@ -833,10 +925,19 @@ __global__ void __launch_bounds__(TcShape<D, NQ>::kThreads, TcShape<D, NQ>::kCta
                     if (og >= G) og -= G, ++otok;
                 }
             }
-            const uint32_t again = __ballot_sync(0xffffffffu, live && odd);
-            if (again) {
-                __syncwarp();
-                tc_redo_rows<T, D>(a, t, kvh, k0, k1, part, warp * 32, again);
+            odd = odd && live && l == l;
+            if (__any_sync(0xffffffffu, odd)) {
+                int lo = 0, hi = c.base;
+                const uint32_t *words = nullptr;
+                if (a.tree_mask) words = a.tree_mask + (size_t)(c.q0 + tok) * a.mask_words;
+                else ext_row_range(a, c.prefix, pos, lo, hi);
+                const int how = tc_not_its_own<T, D>(a, c, t.seq, kvh, odd && nan, odd && !nan, lo, hi, words);
+                const uint32_t again = __ballot_sync(0xffffffffu, how != 0);
+                const uint32_t small = __ballot_sync(0xffffffffu, how == 2);
+                if (again) {
+                    __syncwarp();
+                    tc_redo_rows<T, D>(a, t, kvh, k0, k1, part, warp * 32, again, small);
+                }
             }
         }
     }
