@@ -71,6 +71,9 @@ struct TcShape {
     static constexpr int kThreads = kRows + 32 + NQ * 32;
     static constexpr int kTiles = NQ * kQBytes + (NK + NV) * kTileBytes;  // then TcControl
     static_assert(kOCol + NQ * D <= 512, "TMEM columns");
+    // the product warps' order: score tiles ahead of one row tile's outputs, or two row
+    // tiles in turn with one score tile each
+    static_assert((NQ == 1 && NS == 2) || (NQ == 2 && NS == 1), "score tiles");
 };
 
 struct TcControl {
@@ -702,12 +705,6 @@ __global__ void __launch_bounds__(TcShape<D, NQ>::kThreads, TcShape<D, NQ>::kCta
                 if (two) mbar_arrive(&c.turn[q]);
             }
             __syncwarp();
-            if (NQ == 1 && NS == 1 && more) {
-                wait_k(j + 1);
-                tc_fence_after();
-                if (ok && elect_one()) scores(j + 1);
-                __syncwarp();
-            }
         }
         if (!ok && q * 128 < t.nrows) {  // given up: the products issued must end before TMEM goes
             if (elect_one()) mma_commit(&c.o_full[q]);
