@@ -427,9 +427,9 @@ pkv_status pkv_paged_attention_decode_shared_prefix_run(
  *   that lies wholly before every token's window is not looked at.
  * query_starts: device int32 [num_seqs + 1], non-decreasing, within
  *   [0, num_tokens].  max_query_len, max_context_len: host upper bounds.
- * softcap: 0 = none (scale / softcap must be finite in fp32).  window: 0 = none.  alibi_slopes: device float
- *   [num_heads] or NULL.  prefix_lens: device int32 [num_seqs] or NULL,
- *   taken within [0, context length].
+ * softcap: 0 = none (scale / softcap must be finite in fp32).  window: 0 =
+ *   none.  alibi_slopes: device float [num_heads] or NULL.  prefix_lens: device
+ *   int32 [num_seqs] or NULL, taken within [0, context length].
  * partition_tokens: 0 = automatic, -1 = never split, > 0 = split the keys
  *   that a tile of rows sees into parts of this many (a multiple of
  *   block_size, at most 8192), joined by a log-sum-exp pass.  workspace: at
@@ -457,7 +457,8 @@ pkv_status pkv_paged_attention_decode_shared_prefix_run(
  *   weights of 16-bit pools meet the values in the pool's type: rounded once
  *   where out_dtype has 16 bits (half a step of the pool's type, relative to each
  *   weight, which the decode does not round; a token that sees one key still
- *   gets that value bit by bit), as two parts where it is F32.
+ *   gets that value bit by bit, while its score is below some thousands), as
+ *   two parts where it is F32.
  * Supported: BF16 and F16 pools of every head size, F32 pools of head_dim 64
  * and 128; num_heads / num_kv_heads in 1..16.
  */

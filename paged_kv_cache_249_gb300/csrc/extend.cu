@@ -19,18 +19,24 @@ struct alignas(64) MapPair {
     CUtensorMap k, v;
 };
 
-// Automatic split: cut the keys of every tile into parts, of at least
-// kExtMinPart (kExtMinPartFma on the CUDA cores), until the launch has about this many items if all sequences are
-// as long as the longest (a batch usually holds shorter ones).  Where two CTAs
-// share an SM one's start and end hide behind the other, so more and shorter
-// items are taken there.  Measured (us, parts of 512, 1024, 2048, 4096, 8192
-// tokens, none): 32 trees of up to 32 nodes over 512-8192 tokens 247, 178, 145,
-// 128, 160, 151; two of up to 64 nodes over 32768 and 98304 tokens (256-row
-// tiles) 740, 467, 314, 269, 246, 1178.  On the CUDA cores (parts of 64, 128,
-// 256, 512, 1024, none): three sequences of 33-257 tokens over up to 500 more
-// 40, 45, 56, 82, 75, 76; one of 512 tokens, head_dim 128, 90, 63, 98, 129, 129,
-// 129; 64 single tokens over 100-2000, head_dim 64 (tiles of 16 rows) 205, 145,
-// 115, 113, 109, 173.
+// Automatic split: cut the keys of every tile into parts, of at least kExtMinPart
+// (kExtMinPartFma on the CUDA cores), until the launch has about this many items if
+// all sequences are as long as the longest (a batch usually holds shorter ones).
+// Where two CTAs share an SM one's start and end hide behind the other, so more and
+// shorter items are taken there.  Measured (us, by part length; "auto" is what these
+// rules take):
+//   tensor cores                      512   1024   2048   4096   8192   none   auto
+//   32 trees of up to 32 nodes over
+//     512-8192                        180    138    115    103    120    108    102
+//   2 of up to 64 over 32768 and
+//     98304 (256-row tiles)           637    410    282    242    219   1071    213
+//   CUDA cores                         64    128    256    512   1024   none   auto
+//   3 sequences of 33-257 tokens over
+//     up to 500 more, head_dim 64    35.6   42.9   51.6   78.3   72.9   72.2   42.6
+//   one of 512 tokens, head_dim 128  81.1   62.9   94.1    117    117    117   62.4
+//   64 single tokens over 100-2000,
+//     head_dim 64 (16-row tiles)     95.8   69.3   64.8   62.1    106    163   62.1
+// (Parts of 64 would serve the first of the last three and cost the others.)
 int tile_count(long long num_tokens, int num_seqs, int group, int rows) {
     return (int)(num_tokens * group / rows) + num_seqs;
 }
@@ -48,10 +54,11 @@ long long most_parts(int rows, long long range) {
 // Parts of the automatic split for a range of `range` keys.  Within the bounds
 // above, as many as make the sum of two times least: a part's keys, one after
 // another in a CTA, and the joining pass, which reads and writes every part of
-// every row.  In us, measured on single CTAs and joining passes: D / 12800 a key
-// (CUDA cores: D / 1100), and 3 + D / 625000 for a part of a row.  (One sequence
-// of 300 tokens 9.7 us unsplit, 16.9 in two parts; three of 100 over up to 1000
-// 15.4 and 21.8.)
+// every row.  In us, measured on single CTAs and joining passes: D / 12800 a key,
+// and 3 + D / 625000 for a part of a row.  (One sequence of 300 tokens 9.7 us
+// unsplit, 16.9 in two parts; three of 100 over up to 1000 15.4 and 21.8.)  On the
+// CUDA cores D / 1100 a key is not what a CTA alone takes (D / 610), but chooses
+// well among the parts above.
 int auto_parts(long long num_tokens, int num_seqs, int num_heads, int num_kv_heads, int rows,
                int head_dim, long long range) {
     const long long tiles =

@@ -14,8 +14,9 @@
 // feed 96 or 128 multiply-adds, so that full the kernel does 32 TFLOP/s of 74 (8
 // sequences of 1024 tokens, 32 heads of 128: 2.17 ms); 8 by 8 would leave one
 // CTA of four warps on an SM.  Small calls are bound by a tile's latency
-// instead: a warp per scheduler issues an instruction in 2.8 clocks, 64 keys take
-// 4 us (D = 64), so that keys are split over many CTAs.  Keys and values are
+// instead: alone on an SM, with a warp per scheduler that issues an instruction in
+// 2.8 clocks, it takes 6.7 us for 64 keys (D = 64; 12.0 at 128), so that keys are
+// split over many CTAs.  Keys and values are
 // copied in asynchronously: the next tile's keys beside this one's weights, its
 // values beside the next scores.
 

@@ -16,12 +16,12 @@
 //
 // What bounds it, as measured:
 //   - few rows, long ranges (single tokens, trees): HBM.  64 single tokens over
-//     512-8192 with 256-wide heads and capped scores 338 us, 6.7 TB/s; 32 trees
-//     of up to 32 nodes over 512-8192 107 us, 5.5 TB/s (6.0 in the kernel; the
+//     512-8192 with 256-wide heads and capped scores 328 us, 6.9 TB/s; 32 trees
+//     of up to 32 nodes over 512-8192 108 us, 5.4 TB/s (6.1 in the kernel; the
 //     rest is the joining pass and the CTAs' ends).
 //   - many rows: softmax and products of a row tile follow each other, and two
 //     row tiles share an SM.  Three prompts of 2048-6144 tokens, 32 heads of
-//     128: 385 us, 1.25 PFLOP/s, tensor pipe 57 % busy.  Per 128 keys and row
+//     128: 381 us, 1.26 PFLOP/s, tensor pipe 57 % busy.  Per 128 keys and row
 //     tile the softmax takes 1700 cycles (two readings of the scores 600, the
 //     exponentials 1000) and the products 1300 at the rate that a large GEMM
 //     reaches; the first half of P V runs beside the softmax.
